@@ -27,6 +27,7 @@
 
 #include <float.h>
 
+#include "beam_list.h"
 #include "kv_device.h"
 
 namespace qmvd {
@@ -34,7 +35,6 @@ namespace qmvd {
 constexpr int kBeamMost = 32;                  // `num` at most (fewer than a wave's lanes)
 constexpr int kScanThreads = 256;
 constexpr int kScanWaves = kScanThreads / 64;
-constexpr int kScanList = 1024;                // logits of a chunk that are ranked
 
 struct BeamArgs {
   const void *logits;                          // [B, W, V] bf16 or fp32, row stride logits_ld
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(BeamArgs a) {
       mine += __popc(hits[p]);
     }
     int i = atomicAdd(&count, mine);
-    if (i + mine <= kScanList) {
+    if (list_fits(i, mine)) {
 #pragma unroll
       for (int p = 0; p < PER / 16; ++p) {
         for (uint32_t bits = hits[p]; bits != 0; bits &= bits - 1) {   // one or two in all
@@ -228,9 +228,9 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(BeamArgs a) {
   const int n = count;
   // as keys, the logits read again (they are in the cache); zeros among them
   // are no entries
-  for (int i = tid; i < min(n, kScanList); i += kScanThreads) {
-    const int f = static_cast<int>(found[i]);
-    const uint64_t key = f < len ? rank_key(logit_at(a, row, v0 + f), v0 + f) : 0;
+  for (int i = tid; i < list_readable(n); i += kScanThreads) {
+    const uint32_t f = found[i];
+    const uint64_t key = f < static_cast<uint32_t>(len) ? rank_key(logit_at(a, row, v0 + f), v0 + f) : 0;
     list[i] = key >= cut ? key : 0;
   }
   __syncthreads();

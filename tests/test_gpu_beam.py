@@ -183,3 +183,16 @@ def test_many_logits_above_the_bound(dev):
         x = torch.where(at // 8 % 64 < num + 1, x * 4 + 10, x)
         x = x if f32 else x.to(torch.bfloat16)
         _check(dev, x, np.zeros((1, W), np.float32), num, f32)
+
+
+def test_equal_logits_that_overflow_one_list(dev):
+    """A row of equal logits whose last chunk has 1105 of them: one thread's
+    single logit is past the list's end, where the others' do not fit."""
+    import torch
+    for V in (50257, 1025, 1040, 2049, 4096 + 1105):
+        for f32 in (True, False):
+            x = torch.zeros(2, V, device=dev, dtype=torch.float32 if f32 else torch.bfloat16).view(1, 2, V)
+            for num in (1, 32):
+                got, par, tok = _select(dev, x, np.zeros((1, 2), np.float32), num)
+                assert np.all(par == 0) and np.array_equal(tok[0], np.arange(num)), (V, f32, num)
+                np.testing.assert_allclose(got, -np.log(V), rtol=0, atol=2.0 ** -20 * (1 + np.log(V)))
