@@ -4,6 +4,7 @@
 
 #include <float.h>
 
+#include "append_quick.h"
 #include "kv_device.h"
 
 namespace qmvd {
@@ -106,18 +107,15 @@ struct Quantized {
       s = edge / q0;
       z = edge;
     }
-    // q = min(round((x - z) / s), top), the quotient rounded to fp32 first.
-    // x / s - z / s by the reciprocal of s is off by less than 3 units of 2^-23
-    // of the largest code, that quotient's own roundings included: wherever it
-    // is further than four from a half, rounding it gives the same code, and
-    // elsewhere (one lane in 500 at 8 bits) the divisions are done.
-    constexpr float kNear = static_cast<float>(1 << BITS) / (1 << 21);
-    const float inverse = __builtin_amdgcn_rcpf(s), shift = -z * inverse;
+    // q = min(round((x - z) / s), top), by the reciprocal of s where that is sure
+    // to give the same code (append_quick.h)
+    constexpr float kNear = quick_near(BITS);
+    const float inverse = __builtin_amdgcn_rcpf(s);
     uint32_t byte[2] = {0u, 0u};
     float far = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float r = fmaf(x[e], inverse, shift);
+      const float r = quick_quotient(x[e], z, inverse);
       far = fmaxf(far, fabsf(r - __builtin_rintf(r)));
       byte[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(BITS == 8 ? r : fminf(r, top), e % 4, byte[e / 4]);   // 0 to 255
     }

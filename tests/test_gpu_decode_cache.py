@@ -308,3 +308,53 @@ def test_append_codes_equal_the_quantizer_in_bulk(dev, bits, gs):
         for t, want in zip(pool, (wq.view(np.int32), sc.view(np.int16), bi.view(np.int16))):
             got = _bits(t[at].transpose(1, 2).reshape(16 * page, heads, -1)[:T])
             np.testing.assert_array_equal(got.reshape(T * heads, -1), want)
+
+
+def _groups_near_halves(bits, gs):
+    """bf16 patterns [n, gs]: every pair of a largest value in [1, 2) and a
+    smallest one up to 200 steps below it, with the values between them whose
+    quotients come closest to a half."""
+    top = np.float32((1 << bits) - 1)
+    value = lambda p: (p.astype(np.uint32) << 16).view(np.float32)  # noqa: E731
+    out = []
+    for hi in range(0x3F80, 0x4000):
+        lo = np.arange(hi - 200, hi)
+        h, low = value(np.full(200, hi)), value(lo)
+        s = -((h - low) / top)
+        s = h / np.trunc(h / s - np.float32(0.5))                         # rounded away from zero, as it is negative
+        x = np.arange(hi - 200, hi + 1)
+        q = ((value(x) - h[0])[None] / s[:, None]).astype(np.float64)
+        far = np.where(x[None] >= lo[:, None], np.abs(q - np.floor(q) - 0.5), 9.0)
+        take = np.argsort(far, 1, kind="stable")[:, :gs - 2]
+        pick = np.where(np.take_along_axis(far, take, 1) < 1.0, x[take], hi)
+        out.append(np.concatenate([np.full((200, 1), hi), lo[:, None], pick], 1))
+    return np.concatenate(out).astype(np.uint16)
+
+
+@pytest.mark.parametrize("bits,gs", [(8, 32), (8, 64), (8, 128), (4, 32), (4, 64), (4, 128)])
+def test_append_codes_of_groups_without_a_zero(dev, bits, gs):
+    """Groups whose values all lie above zero (or all below), one to 200 bf16
+    steps apart: the bias is many times the range away.  Among their quotients
+    are those closest to a half, where a code changes."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    heads, D, page = 4, 128, 64
+    groups = _groups_near_halves(bits, gs)
+    T = len(groups) * gs // (2 * heads * D)
+    rng = np.random.default_rng(bits + gs)
+    groups = groups[rng.permutation(len(groups))[:T * 2 * heads * D // gs]]
+    groups = np.where(rng.random((len(groups), 1)) < 0.1, groups ^ 0x8000, groups)
+    x = torch.from_numpy(groups.astype(np.uint16).view(np.int16).reshape(T, 2 * heads, D)).view(torch.bfloat16)
+    pages = -(-T // page)
+    tables = rng.permutation(pages + 1)[None, :pages].astype(np.int32)
+    cache = ref.Cache(dev, pages + 1, heads, page, D, bits, gs)
+    xd = x.to(dev)
+    qm.qmv_kv_append(xd[:, :heads], xd[:, heads:], cache.k, cache.v, torch.from_numpy(tables).to(dev),
+                     torch.arange(T, dtype=torch.int32, device=dev), rows=torch.zeros(T, dtype=torch.int32, device=dev), **cache.kw)
+    at = torch.from_numpy(tables[0].astype(np.int64)).to(dev)
+    for pool, src in ((cache.k, x[:, :heads]), (cache.v, x[:, heads:])):
+        wq, sc, bi = oracle.quantize_pack(src.float().numpy().reshape(T * heads, D), gs, bits)
+        for t, want in zip(pool, (wq.view(np.int32), sc.view(np.int16), bi.view(np.int16))):
+            got = _bits(t[at].transpose(1, 2).reshape(pages * page, heads, -1)[:T])
+            np.testing.assert_array_equal(got.reshape(T * heads, -1), want)
