@@ -13,9 +13,13 @@ Any strides will do as long as a row is contiguous and all tensors of a cache
 have the same strides in rows, so [pages, page_size, heads, head_dim] memory is
 passed as its ``transpose(1, 2)`` view.  ``block_tables`` is int32 [B, columns]:
 slot t of sequence b lies in page ``block_tables[b, t // page_size]``.
+
+With ``stream`` a call's kernels run there, and what it allocates itself
+(workspace, results) belongs to that stream, as under ``torch.cuda.stream``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import struct
@@ -184,6 +188,13 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _owner(stream):
+    """Where a call's own allocations have to be made: memory of the current
+    stream's pool may be in use there, and is handed out there again as soon as
+    a workspace is dropped, whatever another stream is still doing with it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -312,11 +323,12 @@ def qmv_kv_attend(q, k_cache, v_cache, block_tables, lengths, scale=None, mask=N
         _spec(block_tables, "block_tables"), _spec(lengths, "lengths"), _spec(mask, "mask"), _spec(weights, "weights"),
         _spec(weights_out, "weights_out"), _spec(y, "y"), out_dtype, _spec(workspace, "workspace"), group_size, bits, most)
     device = q.device
-    if y is None:
-        y = q.new_empty(q.shape, dtype=dtype)
-    lse = q.new_empty(q.shape[:2], dtype=_F32) if return_lse else None
-    if workspace is None and need:
-        workspace = q.new_empty(need, dtype=_U8)
+    with _owner(stream):
+        if y is None:
+            y = q.new_empty(q.shape, dtype=dtype)
+        lse = q.new_empty(q.shape[:2], dtype=_F32) if return_lse else None
+        if workspace is None and need:
+            workspace = q.new_empty(need, dtype=_U8)
     if weights_out is None:
         weights_out = weights
     _call("qmv_kv_attend", q.data_ptr(), q.stride(0), q.stride(1), _cache(k_cache, v_cache, dims),
@@ -372,10 +384,11 @@ def qmv_kv_evict(k_cache, v_cache, block_tables, lengths, weights, positions, ne
         None if out is None else tuple(_spec(t, "out") for t in out), _spec(workspace, "workspace"), group_size, bits,
         budget)
     device, shape = weights.device, weights.shape
-    if out is None:
-        out = lengths.new_empty(B), weights.new_empty(shape), positions.new_empty(shape)
-    if workspace is None:
-        workspace = weights.new_empty(need, dtype=_U8)
+    with _owner(stream):
+        if out is None:
+            out = lengths.new_empty(B), weights.new_empty(shape), positions.new_empty(shape)
+        if workspace is None:
+            workspace = weights.new_empty(need, dtype=_U8)
     _call("qmv_kv_evict", _cache(k_cache, v_cache, dims), block_tables.data_ptr(), *table, lengths.data_ptr(), B,
           weights.data_ptr(), positions.data_ptr(), *meta, next_positions.data_ptr(), budget, recent, out[0].data_ptr(),
           out[1].data_ptr(), out[2].data_ptr(), workspace.data_ptr(), _size(workspace), _stream(stream, device))
@@ -415,11 +428,12 @@ def qmv_beam_select(logits, scores, num: int, out=None, workspace=None, stream=N
         _spec(logits, "logits"), _spec(scores, "scores"), num,
         None if out is None else tuple(_spec(t, "out") for t in out), _spec(workspace, "workspace"))
     device = logits.device
-    if out is None:
-        shape = (sizes[0], num)
-        out = scores.new_empty(shape), scores.new_empty(shape, dtype=_I32), scores.new_empty(shape, dtype=_I32)
-    if workspace is None:
-        workspace = scores.new_empty(need, dtype=_U8)
+    with _owner(stream):
+        if out is None:
+            shape = (sizes[0], num)
+            out = scores.new_empty(shape), scores.new_empty(shape, dtype=_I32), scores.new_empty(shape, dtype=_I32)
+        if workspace is None:
+            workspace = scores.new_empty(need, dtype=_U8)
     _call("qmv_beam_select", logits.data_ptr(), *form, scores.data_ptr(), *sizes, num, out[0].data_ptr(),
           out[1].data_ptr(), out[2].data_ptr(), workspace.data_ptr(), _size(workspace), _stream(stream, device))
     return out
@@ -456,8 +470,9 @@ def qmv_beam_reorder(k_cache, v_cache, block_tables, lengths, parents, spare_pag
         _spec(lengths, "lengths"), _spec(parents, "parents"), _spec(spare_pages, "spare_pages"),
         None if out is None else tuple(_spec(t, "out") for t in out), group_size, bits)
     device = lengths.device
-    if out is None:
-        out = lengths.new_empty((sizes[0], par[1], sizes[2])), lengths.new_empty((sizes[0], par[1]))
+    with _owner(stream):
+        if out is None:
+            out = lengths.new_empty((sizes[0], par[1], sizes[2])), lengths.new_empty((sizes[0], par[1]))
     _call("qmv_beam_reorder", _cache(k_cache, v_cache, dims), block_tables.data_ptr(), lengths.data_ptr(), *sizes,
           parents.data_ptr(), *par, spare_pages.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), _stream(stream, device))
     return out
