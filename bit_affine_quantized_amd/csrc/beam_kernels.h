@@ -11,8 +11,8 @@
 // a rounding apart can share one c, and then the index decides, so a logit
 // just below a chunk's list could still win.  Each chunk reports the best
 // logit it left out; beam_join_kernel, which joins the sums, ranks the lists
-// and sees the threshold, takes the slow exact way where that logit ties with
-// the threshold ahead of a listed one.
+// and sees the threshold, takes the slow exact way where a logit left out could
+// tie with the threshold ahead of a listed one.
 //
 // On MI355X, 16 items x 8 beams x 131072 tokens, bf16 (33.6 MB): 15.8 us for the
 // scan, of which the loads take about 4 and vector instructions the rest: all
@@ -298,6 +298,24 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t *slots) {
   return v;
 }
 
+// The next logit below a finite x that the logits' type can hold.
+__device__ __forceinline__ float just_below(float x, bool f32) {
+  const uint32_t u = __float_as_uint(x), step = f32 ? 1u : 0x10000u;
+  return __uint_as_float(x > 0.0f ? u - step : x < 0.0f ? u + step : 0x80000000u + step);
+}
+
+// Whether a chunk that left `next` out, as the best of what its full list does
+// not hold, may hold a logit below `next` with next's score c.  c does not fall
+// where x rises, so the one just below decides.  In a row whose lse is NaN every
+// logit's c is -infinity.  Nothing ranks below NaN, and in a row with a number
+// for lse, so without NaN, nothing below -infinity.
+__device__ __forceinline__ bool lower_ties(float score, float next, float lse, bool f32) {
+  if (next != next) return false;
+  if (lse != lse) return true;
+  return next != -INFINITY &&
+         ordered(candidate(score, just_below(next, f32), lse)) == ordered(candidate(score, next, lse));
+}
+
 // One workgroup per batch item.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
   extern __shared__ float lse[];               // [W], then the scores [W]
@@ -382,7 +400,8 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
     __syncthreads();
     // a logit that no list holds, yet ties with the threshold ahead of a
     // listed one: it lies in a chunk whose list is full, at or below the best
-    // logit left out there, and a larger listed logit has the same c
+    // logit left out there.  Where it equals that one, the listed logits equal to
+    // it come first, and only a larger listed one with the same c may not.
     const uint32_t t = static_cast<uint32_t>(winner_min >> 32);
     for (int i = tid; i < a.W * a.chunks; i += kJoinThreads) {
       const int w = static_cast<int>(div_by(static_cast<uint32_t>(i), a.per_chunk));
@@ -390,6 +409,7 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
       const float next = a.left_out[row0 * a.chunks + i];
       if (mine[a.num - 1][1] == ~0u) continue;
       if (ordered(candidate(score[w], next, lse[w])) != t) continue;
+      if (lower_ties(score[w], next, lse[w], a.f32)) slow = 1;
       for (int j = 0; j < a.num; ++j) {
         const float x = __uint_as_float(mine[j][0]);
         if (!(x == next) && ordered(candidate(score[w], x, lse[w])) == t) slow = 1;

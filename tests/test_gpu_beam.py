@@ -196,3 +196,52 @@ def test_equal_logits_that_overflow_one_list(dev):
                 got, par, tok = _select(dev, x, np.zeros((1, 2), np.float32), num)
                 assert np.all(par == 0) and np.array_equal(tok[0], np.arange(num)), (V, f32, num)
                 np.testing.assert_allclose(got, -np.log(V), rtol=0, atol=2.0 ** -20 * (1 + np.log(V)))
+
+
+def _by_definition(x, scores, num):
+    """(beams, tokens) by fp32 steps on the given fp32 logits, for rows whose
+    log-sum-exp is NaN or far above the logits' differences."""
+    B, W, V = x.shape
+    with np.errstate(invalid="ignore"):
+        m = x.max(-1, keepdims=True)
+        lse = (m + np.log(np.exp((x - m).astype(np.float64)).sum(-1, keepdims=True))).astype(np.float32)
+        c = scores[..., None] + (x - lse)
+    c = np.where(np.isnan(c), -np.inf, c).reshape(B, W * V)
+    at = np.argsort(-c, axis=-1, kind="stable")[:, :num]
+    return at // V, at % V
+
+
+def test_a_row_with_a_nan_among_equal_logits(dev):
+    """Its log-sum-exp is NaN, so every candidate counts as -infinity and the
+    lowest indices win, the NaN's own among them."""
+    import torch
+    for V in (40, 9000, 50257):
+        for f32 in (True, False):
+            for bad in (float("nan"), float("inf"), float("-inf")):
+                for where in ([0], [3], list(range(0, 40, 2)), [V - 1]):
+                    for W in (1, 2):                       # a second beam of nothing but NaN
+                        x = torch.full((1, W, V), float("nan"), device=dev)
+                        x[0, 0] = 1.5
+                        x[0, 0, where] = bad
+                        x = x if f32 else x.to(torch.bfloat16)
+                        scores = np.array([[0.0, 5.0]], np.float32)[:, :W]
+                        got, par, tok = _select(dev, x, scores, 5)
+                        want = _by_definition(x.float().cpu().numpy(), scores, 5)
+                        assert np.array_equal(par, want[0]) and np.array_equal(tok, want[1]), (V, f32, bad, where[0], W, tok)
+                        if bad != float("-inf"):
+                            assert np.all(got == -np.inf)
+
+
+def test_lower_logits_that_round_to_equal_ones_scores(dev):
+    """More equal logits than a list holds, and before them others a rounding
+    lower: all have one score, so the lowest indices win."""
+    import torch
+    for V in (300, 9000):
+        for f32 in (True, False):
+            x = torch.full((1, 2, V), 2.0 ** -30, device=dev)
+            x[0, :, :7] = 2.0 ** -31
+            x[0, :, 20:25] = -2.0 ** -30
+            x = x if f32 else x.to(torch.bfloat16)
+            for num in (1, 4, 12):
+                _, par, tok = _select(dev, x, np.full((1, 2), -1.0, np.float32), num)
+                assert np.all(par == 0) and np.array_equal(tok[0], np.arange(num)), (V, f32, num, tok)
