@@ -11,8 +11,11 @@
 // a rounding apart can share one c, and then the index decides, so a logit
 // just below a chunk's list could still win.  Each chunk reports the best
 // logit it left out; beam_join_kernel, which joins the sums, ranks the lists
-// and sees the threshold, takes the slow exact way where a logit left out could
-// tie with the threshold ahead of a listed one.
+// and sees the threshold, goes through the logits for the entries that tie with
+// it where one left out could do so ahead of a listed one.  Everything above the
+// threshold is listed, so one sweep in index order is enough, and it ends with the
+// last entry found: at once for a finished item, whose beams' scores are all
+// -infinity.
 //
 // On MI355X, 16 items x 8 beams x 131072 tokens, bf16 (33.6 MB): 15.8 us for the
 // scan, of which the loads take about 4 and vector instructions the rest: all
@@ -323,11 +326,12 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
   __shared__ uint64_t list[kJoinList];
   __shared__ uint64_t slots[kJoinWaves];
   __shared__ uint64_t winner_min;
-  __shared__ int count, slow;
+  __shared__ uint32_t sums[kJoinWaves];
+  __shared__ int count, tie, above;
   const int b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row0 = static_cast<int64_t>(b) * a.W;
-  if (tid == 0) count = slow = 0;
+  if (tid == 0) count = tie = above = 0;
   // the entries of the lists that a thread holds itself, on their way early
   const int total = a.W * a.chunks * a.num;
   const u32x2 *entries = a.list + row0 * a.chunks * a.num;
@@ -381,7 +385,23 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
     });
   }
   __syncthreads();
-  const int n = count;
+  int n = count;
+  if (__builtin_expect(n > kJoinList, 0)) {    // a few threads hold most of the entries: the winners one by one
+    uint64_t last = ~uint64_t(0);
+    for (int r = 0; r < a.num; ++r) {
+      uint64_t top = 0;
+#pragma nounroll
+      for (int i = tid; i < total; i += kJoinThreads) {
+        const uint64_t k = key_of(i, entries[i]);
+        top = k < last && k > top ? k : top;
+      }
+      top = block_max(top, slots);
+      if (tid == 0) list[r] = top;
+      last = top;
+    }
+    n = a.num;
+    __syncthreads();
+  }
   const int64_t out = static_cast<int64_t>(b) * a.num;
   auto write = [&](int rank, uint64_t key) {
     const uint32_t i = key_index(key), w = i / static_cast<uint32_t>(a.V);
@@ -389,49 +409,69 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamArgs a) {
     a.out_parents[out + rank] = static_cast<int32_t>(w);
     a.out_tokens[out + rank] = static_cast<int32_t>(i - w * static_cast<uint32_t>(a.V));
   };
-  if (n <= kJoinList) {
-    for (int i = tid; i < n; i += kJoinThreads) {
-      const uint64_t key = list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += list[j] > key;
-      if (rank < a.num) write(rank, key);
-      if (rank == a.num - 1) winner_min = key;
-    }
-    __syncthreads();
-    // a logit that no list holds, yet ties with the threshold ahead of a
-    // listed one: it lies in a chunk whose list is full, at or below the best
-    // logit left out there.  Where it equals that one, the listed logits equal to
-    // it come first, and only a larger listed one with the same c may not.
-    const uint32_t t = static_cast<uint32_t>(winner_min >> 32);
-    for (int i = tid; i < a.W * a.chunks; i += kJoinThreads) {
-      const int w = static_cast<int>(div_by(static_cast<uint32_t>(i), a.per_chunk));
-      const u32x2 *mine = a.list + (row0 * a.chunks + i) * a.num;
-      const float next = a.left_out[row0 * a.chunks + i];
-      if (mine[a.num - 1][1] == ~0u) continue;
-      if (ordered(candidate(score[w], next, lse[w])) != t) continue;
-      if (lower_ties(score[w], next, lse[w], a.f32)) slow = 1;
-      for (int j = 0; j < a.num; ++j) {
-        const float x = __uint_as_float(mine[j][0]);
-        if (!(x == next) && ordered(candidate(score[w], x, lse[w])) == t) slow = 1;
-      }
-    }
-    __syncthreads();
-    if (!slow) return;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const uint64_t key = list[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += list[j] > key;
+    if (rank < a.num) write(rank, key);
+    if (rank == a.num - 1) winner_min = key;
   }
-  // the slow way: one sweep over all candidates for each winner
-  uint64_t last = ~uint64_t(0);
-  const int64_t every = static_cast<int64_t>(a.W) * a.V;
-  for (int r = 0; r < a.num; ++r) {
-    uint64_t top = 0;
-    for (int64_t i = tid; i < every; i += kJoinThreads) {
-      const int w = static_cast<int>(i / a.V), v = static_cast<int>(i - static_cast<int64_t>(w) * a.V);
-      const uint64_t k = rank_key(candidate(a.scores[row0 + w], logit_at(a, row0 + w, v), lse[w]),
-                                  static_cast<uint32_t>(i));
-      if (k < last && k > top) top = k;
+  __syncthreads();
+  // a logit that no list holds, yet ties with the threshold ahead of a
+  // listed one: it lies in a chunk whose list is full, at or below the best
+  // logit left out there.  Where it equals that one, the listed logits equal to
+  // it come first, and only a larger listed one with the same c may not.
+  const uint32_t t = static_cast<uint32_t>(winner_min >> 32);
+  for (int i = tid; i < a.W * a.chunks; i += kJoinThreads) {
+    const int w = static_cast<int>(div_by(static_cast<uint32_t>(i), a.per_chunk));
+    const u32x2 *mine = a.list + (row0 * a.chunks + i) * a.num;
+    const float next = a.left_out[row0 * a.chunks + i];
+    if (mine[a.num - 1][1] == ~0u) continue;
+    if (ordered(candidate(score[w], next, lse[w])) != t) continue;
+    if (lower_ties(score[w], next, lse[w], a.f32)) tie = 1;
+    for (int j = 0; j < a.num; ++j) {
+      const float x = __uint_as_float(mine[j][0]);
+      if (!(x == next) && ordered(candidate(score[w], x, lse[w])) == t) tie = 1;
     }
-    top = block_max(top, slots);
-    if (tid == 0) write(r, top);
-    last = top;
+  }
+  __syncthreads();
+  if (__builtin_expect(!tie, 1)) return;
+  for (int i = tid; i < n; i += kJoinThreads)
+    if (static_cast<uint32_t>(list[i] >> 32) > t) atomicAdd(&above, 1);
+  __syncthreads();
+  // in the ranks below those, the lowest indices that tie, eight logits a thread
+  // at a time
+  int filled = above;
+  for (int w = 0; w < a.W && filled < a.num; ++w) {
+    const float of = score[w], by = lse[w];
+    for (int64_t v0 = 0; v0 < a.V && filled < a.num; v0 += 8 * kJoinThreads) {
+      const int64_t v = v0 + 8 * tid;
+      float x[8];
+      if (v + 8 <= a.V) {
+        load8(a, (row0 + w) * a.logits_ld + v, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v + e < a.V ? logit_at(a, row0 + w, static_cast<int>(v) + e) : 0.0f;
+      }
+      uint32_t hits = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) hits |= (v + e < a.V && ordered(candidate(of, x[e], by)) == t ? 1u : 0u) << e;
+      const uint32_t mine = __popc(hits), upto = wave_scan(mine);
+      if (lane == 63) sums[wave] = upto;
+      __syncthreads();
+      int at = filled + static_cast<int>(upto - mine);
+#pragma unroll
+      for (int j = 0; j < kJoinWaves; ++j) {
+        at += j < wave ? static_cast<int>(sums[j]) : 0;
+        filled += static_cast<int>(sums[j]);
+      }
+      for (; hits != 0 && at < a.num; hits &= hits - 1, ++at) {
+        const uint32_t i = static_cast<uint32_t>(w) * static_cast<uint32_t>(a.V) + static_cast<uint32_t>(v) +
+                           static_cast<uint32_t>(__ffs(static_cast<int>(hits)) - 1);
+        write(at, (static_cast<uint64_t>(t) << 32) | (0xFFFFFFFFu - i));
+      }
+      __syncthreads();                         // sums have been read
+    }
   }
 }
 

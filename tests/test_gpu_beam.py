@@ -245,3 +245,85 @@ def test_lower_logits_that_round_to_equal_ones_scores(dev):
             for num in (1, 4, 12):
                 _, par, tok = _select(dev, x, np.full((1, 2), -1.0, np.float32), num)
                 assert np.all(par == 0) and np.array_equal(tok[0], np.arange(num)), (V, f32, num, tok)
+
+
+def test_ties_found_across_rows_and_past_one_sweep_step(dev):
+    """Ties whose lowest indices lie late in a row, at a row's ragged end and in
+    the next rows, behind winners that the lists hold."""
+    import torch
+    B, W, V = 1, 3, 20003
+    for f32 in (True, False):
+        x = torch.full((B, W, V), -30.0, device=dev)
+        for w, where in ((0, [9000, 9001, 16383, 20002]), (1, [0, 7, 8, 12345]), (2, list(range(5000, 5100)))):
+            x[0, w, where] = 2.0 ** -30
+        x[0, 2, 100:104] = 2.0 ** -31                          # a rounding lower, the same score, left out of a full list
+        x[0, 1, 20000:20002] = 1.0
+        x = x if f32 else x.to(torch.bfloat16)
+        # scores that bring every row's ties to one value: two rows a whole number of steps apart would not do
+        lse = torch.logsumexp(x.double(), -1)
+        scores = lse.float() - 8.0
+        for num in (1, 2, 5, 9, 14, 30):
+            _, par, tok = _select(dev, x, scores.cpu().numpy(), num)
+            c = (scores.double()[..., None] + (x.double() - lse[..., None])).reshape(-1).cpu().numpy()
+            c = np.round(c * 2 ** 18)                          # the ties are exact in fp32: 2^-30 is far below a step
+            got = c[par[0].astype(np.int64) * V + tok[0]]
+            assert np.array_equal(got, np.sort(c)[::-1][:num]) and len({*zip(par[0], tok[0])}) == num, (f32, num)
+
+
+def test_few_lanes_hold_most_candidates(dev):
+    """Peaked rows, fifteen strong tokens in every run of 4096: more candidates
+    above the join's bound than it ranks at once."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(8)
+    W, V = 300, 5000
+    x = torch.randn(1, W, V, generator=g, device=dev) * 0.01 - 20
+    for start in (0, 4096):
+        x[0, :, start + 10:start + 25] = torch.rand(W, 15, generator=g, device=dev) * 0.5
+    scores = (-0.25 * np.random.default_rng(3).random((1, W))).astype(np.float32)
+    _check(dev, x, scores, 32, True)
+
+
+def test_a_finished_item_costs_no_more_than_a_live_one(dev):
+    """Scores of -infinity throughout: every candidate ties, and the lowest
+    indices are found at once instead of by sweeps over all logits."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    x = torch.randn(2, 8, 131072, generator=torch.Generator(device=dev).manual_seed(9), device=dev)
+    live = torch.zeros(2, 8, device=dev)
+    done = live.clone()
+    done[1] = float("-inf")
+
+    def best_time(s):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            out = qm.qmv_beam_select(x, s, 16)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times), out
+    t0, _ = best_time(live)
+    t1, (got, par, tok) = best_time(done)
+    assert bool((got[1] == float("-inf")).all()) and bool((par[1] == 0).all()) and tok[1].tolist() == list(range(16))
+    assert t1 < 4 * t0, (t0, t1)
+
+
+def test_late_ties_in_index_order(dev):
+    """One live row: two winners above, then ties from a late index on, of which
+    the lowest ones are a rounding below those that the lists hold."""
+    import torch
+    for V, f32 in ((20003, True), (40001, False), (9000, True)):
+        for W in (1, 3):
+            ties = [8190, 8191, 8192, 8193] + list(range(8300, 8330)) + [V - 2, V - 1]
+            x = torch.full((1, W, V), -30.0, device=dev)
+            x[0, W - 1, ties] = 2.0 ** -30
+            x[0, W - 1, ties[:6]] = 2.0 ** -31
+            x[0, W - 1, [17, V - 5]] = torch.tensor([1.0, 2.0], device=dev)
+            x = x if f32 else x.to(torch.bfloat16)
+            scores = np.full((1, W), -np.inf, np.float32)
+            scores[0, W - 1] = -1.0
+            for num in (1, 2, 3, 5, 11, 30, 32):
+                _, par, tok = _select(dev, x, scores, num)
+                assert np.all(par == W - 1) and tok[0].tolist() == ([V - 5, 17] + ties)[:num], (V, f32, W, num, tok)
