@@ -189,12 +189,19 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(BeamArgs a) {
 
   // The list: `num` logits and the best one left out.  At least that many of
   // a wave's lanes hold a logit at or above `cut`.
-  const uint32_t best = tid * 8 < len && top == top ? ordered(top) : 0u;
+  auto offset = [&](int e) { return ((e >> 3) * kScanThreads + tid) * 8 + (e & 7); };
+  bool none = top != top;                      // NaN alone: no logit of the lane's equals `top`
+  if (top == -INFINITY) {
+    none = true;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) none = none && !(x[e] == top && offset(e) < len);
+  }
+  const uint32_t best = tid * 8 < len && !none ? ordered(top) : 0u;
   const uint64_t cut_w = wave_bound(best, a.num + 1, [&] {
     int first = 0;                             // the lane's first logit that equals `top`
 #pragma unroll
     for (int e = PER - 1; e >= 0; --e) first = x[e] == top ? e : first;
-    return 0xFFFFFFFFu - static_cast<uint32_t>(v0 + ((first >> 3) * kScanThreads + tid) * 8 + (first & 7));
+    return 0xFFFFFFFFu - static_cast<uint32_t>(v0 + offset(first));
   });
   if (lane == 0) {
     wave_m[wave] = m;
@@ -208,21 +215,37 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(BeamArgs a) {
   const float cut_x = cut == 0 ? -INFINITY : key_value(cut);
   if (!(top < cut_x)) {
     uint32_t hits[PER / 16];                   // NaN too: it ranks lowest, but has a rank
-    int mine = 0;
 #pragma unroll
     for (int p = 0; p < PER / 16; ++p) {
       hits[p] = 0;
 #pragma unroll
       for (int e = 15; e >= 0; --e) hits[p] = hits[p] + hits[p] + (x[16 * p + e] < cut_x ? 0u : 1u);
-      mine += __popc(hits[p]);
     }
+    // Where lanes tie at the bound it has an index, or there is no bound: of the
+    // logits at its value only those up to that index (or the chunk's end) are
+    // hits, else the -infinities of a masked vocabulary would overflow the list.
+    if (cut == 0 || static_cast<uint32_t>(cut) != 0) {
+      const uint32_t reach = key_index(cut) - static_cast<uint32_t>(v0);
+      const int last = reach < static_cast<uint32_t>(len) ? static_cast<int>(reach) : len - 1;
+#pragma unroll
+      for (int p = 0; p < PER / 16; ++p) {
+        uint32_t over = 0;
+#pragma unroll
+        for (int e = 15; e >= 0; --e) over = over + over + (x[16 * p + e] > cut_x ? 1u : 0u);
+        const int k0 = min(max(last + 1 - offset(16 * p), 0), 8), k1 = min(max(last + 1 - offset(16 * p + 8), 0), 8);
+        hits[p] &= over | ((1u << k0) - 1) | (((1u << k1) - 1) << 8);
+      }
+    }
+    int mine = 0;
+#pragma unroll
+    for (int p = 0; p < PER / 16; ++p) mine += __popc(hits[p]);
     int i = atomicAdd(&count, mine);
     if (list_fits(i, mine)) {
 #pragma unroll
       for (int p = 0; p < PER / 16; ++p) {
         for (uint32_t bits = hits[p]; bits != 0; bits &= bits - 1) {   // one or two in all
           const int e = 16 * p + __ffs(static_cast<int>(bits)) - 1;
-          found[i++] = static_cast<uint32_t>(((e >> 3) * kScanThreads + tid) * 8 + (e & 7));
+          found[i++] = static_cast<uint32_t>(offset(e));
         }
       }
     }

@@ -327,3 +327,63 @@ def test_late_ties_in_index_order(dev):
             for num in (1, 2, 3, 5, 11, 30, 32):
                 _, par, tok = _select(dev, x, scores, num)
                 assert np.all(par == W - 1) and tok[0].tolist() == ([V - 5, 17] + ties)[:num], (V, f32, W, num, tok)
+
+
+def test_masked_and_equal_rows_cost_no_more(dev):
+    """-infinity in most of the vocabulary, or one value throughout: the ties at
+    a chunk's bound do not overflow its list."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    g = torch.Generator(device=dev).manual_seed(10)
+    x = (torch.randn(16, 8, 131072, generator=g, device=dev) * 2.5).to(torch.bfloat16)
+    s = torch.zeros(16, 8, device=dev)
+    few = torch.full_like(x, float("-inf"))
+    few[:, :, 100:200] = x[:, :, 100:200]
+    half = x.clone()
+    half[:, :, 65536:] = float("-inf")
+
+    def best_time(logits):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            qm.qmv_beam_select(logits, s, 16)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    t0 = best_time(x)
+    for other in (few, half, torch.zeros_like(x)):
+        t = best_time(other)
+        assert t < 3 * t0, (t0, t)
+
+
+@pytest.mark.parametrize("V", [1, 8, 9, 100, 257, 3000, 4096, 4097, 9001])
+@pytest.mark.parametrize("f32", [True, False])
+def test_masked_rows_with_nan_among_them(dev, V, f32):
+    """Few open tokens, -infinity and NaN in every mixture, short rows and short
+    last chunks: what ties at -infinity is taken by its index, NaN's too."""
+    import torch
+    rng = np.random.default_rng(V)
+    for kind in range(8):
+        W = 2
+        x = np.full((1, W, V), -np.inf, np.float32)
+        if kind in (1, 4, 5, 6):                               # a few open, one exact step apart
+            at = rng.permutation(V)[:max(1, min(V, 5 + kind))]
+            x[0, 0, at] = np.arange(len(at), dtype=np.float32) * 0.5
+        if kind in (2, 4):
+            x[0, 0, rng.random(V) < 0.3] = np.nan
+        if kind in (3, 5):
+            x[0, 1] = np.nan
+        if kind == 6:
+            x[0, 1, V // 2:] = np.nan
+        if kind == 7:
+            x[0, :, :V - V // 8] = np.nan
+        scores = np.array([[-1.0, -np.inf if kind == 6 else -2.0]], np.float32)
+        t = torch.from_numpy(x).to(dev)
+        t = t if f32 else t.to(torch.bfloat16)
+        for num in {1, min(4, 2 * V), min(32, 2 * V)}:
+            got, par, tok = _select(dev, t, scores, num)
+            want = _by_definition(x, scores, num)
+            assert np.array_equal(par, want[0]) and np.array_equal(tok, want[1]), (kind, num, par, tok, want)
