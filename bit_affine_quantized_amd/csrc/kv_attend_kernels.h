@@ -155,6 +155,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   bf16x2 r = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
   return __builtin_bit_cast(uint32_t, r);
 }
+// c plus both bf16 values of a pair.
+__device__ __forceinline__ float add_pair(uint32_t pair, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
+}
 // The high halves of a and b, a's in the low half.
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
@@ -379,11 +384,17 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
   }
 
   f32x4 o[OT];
-  float bias_sum[NG];
+  // A probability enters the values' product as the sum of its two terms T, off
+  // by 2^-16 of itself, and a code as what holds it.  That error must not grow
+  // by how far the held codes are from zero, so
+  //   sum p v = sum T (held - kMid) + sum p v_mid,   v_mid the value at the middle code:
+  // the second sum in fp32, the terms' own sum beside it.
+  constexpr float kMid = BITS == 4 ? 188.0f : 127.5f;   // 128 + 8 * 7.5
+  float mid_sum[NG], term_sum[NG];
 #pragma unroll
   for (int j = 0; j < OT; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int g = 0; g < NG; ++g) bias_sum[g] = 0.0f;
+  for (int g = 0; g < NG; ++g) mid_sum[g] = term_sum[g] = 0.0f;
   float m = -INFINITY, l = 0.0f;
   const float lazy = 8.0f * (a.natural == 1.0f ? 0.69314718055994531f : 1.0f);   // a factor of 2^8
   const float *mask = a.mask ? a.mask + b * a.mask_b + hq * a.mask_h : nullptr;
@@ -497,16 +508,20 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
     }
     const bool whole = where.whole();
     if constexpr (CODES) {
-      // 4-bit codes enter the products as 128 + 8 q: scale / 8, bias - 16 scale
+      // 4-bit codes enter the products as 128 + 8 q: scale / 8, and for the keys
+      // bias - 16 scale; the values' bias is taken at the middle code
       float ak[NG], av[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         ak[g] = __uint_as_float(g % 2 == 0 ? affine_k.w[g / 2] << 16 : affine_k.w[g / 2] & 0xFFFF0000u);
         av[g] = __uint_as_float(g % 2 == 0 ? affine_v.w[g / 2] << 16 : affine_v.w[g / 2] & 0xFFFF0000u);
+        const float sv = across_halves(av[g]); // lanes 32..63 get the scales
         if constexpr (BITS == 4) {
-          const float sk = across_halves(ak[g]), sv = across_halves(av[g]);   // lanes 32..63 get the scales
+          const float sk = across_halves(ak[g]);
           ak[g] = lane < 32 ? ak[g] * 0.125f : fmaf(-16.0f, sk, ak[g]);
-          av[g] = lane < 32 ? av[g] * 0.125f : fmaf(-16.0f, sv, av[g]);
+          av[g] = lane < 32 ? av[g] * 0.125f : fmaf(7.5f, sv, av[g]);
+        } else {
+          av[g] = lane < 32 ? av[g] : fmaf(127.5f, sv, av[g]);
         }
         float *ka = reinterpret_cast<float *>(affine + (lane < 32 ? 0 : 1) * kArr);
         float *va = reinterpret_cast<float *>(affine + (lane < 32 ? 2 : 3) * kArr);
@@ -627,7 +642,10 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
 #pragma unroll
       for (int j = 0; j < OT; ++j) o[j] *= alpha;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bias_sum[g] *= alpha;
+      for (int g = 0; g < NG; ++g) {
+        mid_sum[g] *= alpha;
+        term_sum[g] *= alpha;
+      }
     }
     const float base = m == -INFINITY ? 0.0f : m;
     float p[8];
@@ -666,7 +684,7 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
       for (int e = 0; e < 8; ++e) {
         if constexpr (CODES) {
           pg[e] = p[e] * vs[e / 4][e % 4];
-          bias_sum[g] = fmaf(p[e], vb[e / 4][e % 4], bias_sum[g]);
+          mid_sum[g] = fmaf(p[e], vb[e / 4][e % 4], mid_sum[g]);
         } else {
           pg[e] = p[e];
         }
@@ -678,6 +696,10 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
       for (int i = 0; i < 4; ++i) {
         ph[i] = pack_bf16(hi[2 * i], hi[2 * i + 1]);
         if constexpr (HB == 16) pl[i] = pack_bf16(lo[2 * i], lo[2 * i + 1]);
+        if constexpr (CODES) {
+          term_sum[g] = add_pair(ph[i], term_sum[g]);
+          if constexpr (HB == 16) term_sum[g] = add_pair(pl[i], term_sum[g]);
+        }
       }
       qmvk::static_for<0, VPL>([&](auto J) {
         constexpr int j = decltype(J)::value;
@@ -700,7 +722,12 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
   wave_lds_fence();                            // a wave's results replace its tiles
   l = across_rows(l, add);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) bias_sum[g] = across_rows(bias_sum[g], add);
+  for (int g = 0; g < NG; ++g) {
+    mid_sum[g] = across_rows(mid_sum[g], add);
+    term_sum[g] = across_rows(term_sum[g], add);
+    if constexpr (HB == 8) term_sum[g] += __builtin_bit_cast(float, dpp<0x128>(__builtin_bit_cast(uint32_t, term_sum[g])));   // lane ^ 8
+    mid_sum[g] = fmaf(-kMid, term_sum[g], mid_sum[g]);
+  }
   if (kg == 0 && n < HB) {
     join_m(wave, n) = m;
     join_l(wave, n) = l;
@@ -711,7 +738,7 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
     for (int r = 0; r < 4; ++r) {
       float x = o[j][r];
       if constexpr (HB == 8) x += __builtin_bit_cast(float, dpp<0x128>(__builtin_bit_cast(uint32_t, x)));   // lane ^ 8
-      if constexpr (CODES) x += bias_sum[j / VPL];
+      if constexpr (CODES) x += mid_sum[j / VPL];
       if (n < HB) join_o(wave, n)[(j / VPL) * S::GS + VPL * (4 * kg + r) + j % VPL] = x;
     }
   });
