@@ -30,6 +30,7 @@
 
 #pragma once
 
+#include "kv_chunks.h"
 #include "kv_device.h"
 
 namespace qmvd {
@@ -68,7 +69,7 @@ constexpr int kWeightSlots = 512;              // slots a workgroup
 
 constexpr int kTile = 32;                      // tokens a wave takes at a time
 constexpr int kChunkWaves = 4;                 // waves a workgroup that takes a chunk
-constexpr uint32_t kChunkUnit = kChunkWaves * kTile;
+static_assert(kChunkUnit == kChunkWaves * kTile, "a tile for every wave");
 
 // Waves a SIMD that an instance's registers are shared out for: as many as fit
 // without spilling in the loop (bf16 rows are held in registers, codes go
@@ -111,19 +112,15 @@ __device__ __forceinline__ Chunks chunks_of(const AttendArgs &a, int want) {
     c.first = want;
     return c;
   }
-  // in lines of 64 slots: the host keeps all lengths' lines within 2^30
-  constexpr uint32_t kLine = 64;
+  // the host keeps all lengths' lines within 2^30
   auto length = [&](int i) { return i < B ? clamp_length(a.lengths[i], a.max_len) : 0; };
   const int own = length(lane);                // of the first 64 sequences
   uint32_t total = 0;
   for (int i = 0; i < B; i += 64) {
-    const uint32_t lines = ((i == 0 ? own : length(i + lane)) + kLine - 1) / kLine;
+    const uint32_t lines = ((i == 0 ? own : length(i + lane)) + kChunkLine - 1) / kChunkLine;
     total += wave_all(lines, [](uint32_t x, uint32_t y) { return x + y; });
   }
-  const uint32_t line = kChunkUnit / kLine;
-  uint32_t size = (total + a.share - 1) / a.share;
-  size = (size < 1 ? line : (size + line - 1) / line * line) * kLine;
-  const uint32_t most = size > static_cast<uint32_t>(a.most_chunk) ? a.most_chunk : size;
+  const uint32_t most = chunk_slots(total, static_cast<uint32_t>(a.share), static_cast<uint32_t>(a.most_chunk));
   uint32_t before = 0;
   for (int i = 0; i < B; i += 64) {
     const uint32_t len = i == 0 ? own : length(i + lane);
