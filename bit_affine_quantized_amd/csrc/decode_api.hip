@@ -1,5 +1,7 @@
 // C ABI of the decode operators around a paged key-value cache (declared in
 // include/qmv.h): validation before any HIP call, sizing, launch.
+#include <utility>
+
 #include "host_error.h"
 #include "beam_kernels.h"
 #include "kv_attend_launch.h"
@@ -137,6 +139,21 @@ int check_attend(const char *fn, const qmv_kv_cache *c, int64_t B, int64_t cols,
   return QMV_OK;
 }
 
+// Whether slots of a [B, heads, S] array with these strides share memory.
+bool overlapping(int64_t B, int64_t heads, int64_t S, int64_t stride_b, int64_t stride_h) {
+  struct Axis {
+    int64_t size, stride;
+  } axes[2] = {{B, stride_b < 0 ? -stride_b : stride_b}, {heads, stride_h < 0 ? -stride_h : stride_h}};
+  if (axes[0].stride < axes[1].stride) std::swap(axes[0], axes[1]);
+  int64_t run = S;                             // what the inner axes span
+  for (int i = 1; i >= 0; --i) {
+    if (axes[i].size == 1) continue;
+    if (axes[i].stride < run) return true;
+    run = axes[i].stride > INT64_MAX / axes[i].size ? INT64_MAX : (axes[i].size - 1) * axes[i].stride + run;
+  }
+  return false;
+}
+
 int attend(const uint16_t *q, int64_t q_b, int64_t q_h, const qmv_kv_cache *c, const int32_t *tables, int64_t ld,
            int64_t cols, const int32_t *lengths, int64_t B, int group, float scale, const float *mask, int64_t mask_b,
            int64_t mask_h, int64_t mask_cols, const float *weights_in, float *weights_out, int64_t w_b, int64_t w_h,
@@ -159,6 +176,9 @@ int attend(const uint16_t *q, int64_t q_b, int64_t q_h, const qmv_kv_cache *c, c
   if (p.bytes && (!workspace || workspace_bytes < p.bytes))
     return fail(QMV_EINVAL, "%s: workspace of %zu bytes, %zu are needed", fn, workspace ? workspace_bytes : size_t(0), p.bytes);
   if (misaligned(workspace, 16)) return fail(QMV_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  // heads add to their own slots in no order of theirs
+  if (weights && overlapping(B, c->heads, S, w_b, w_h))
+    return fail(QMV_EINVAL, "%s: the slots of weights overlap (strides %lld, %lld)", fn, (long long)w_b, (long long)w_h);
 
   constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -304,8 +304,9 @@ int qmv_kv_append(const uint16_t *k, int64_t k_t, int64_t k_h,
  * head takes no part, whatever its rows hold.  A query head left with no slot
  * gives y = 0 and lse = -infinity.
  * weights_in, weights_out: both NULL, or fp32 [B, heads, S] with strides w_b
- * and w_h (one array may be both): weights_out = weights_in + the attention
- * each slot got, summed over the group's query heads in their order.
+ * and w_h (one array may be both; no two slots in one place): weights_out =
+ * weights_in + the attention each slot got, summed over the group's query heads
+ * in their order.
  * y: [B, heads*group, head_dim], bf16 or fp32.  lse: fp32 [B, heads*group] or
  * NULL.  Scores, probabilities' sums and the weighted values are held in fp32.
  * max_length: the longest length of the call, if the caller knows it (0: the

@@ -149,3 +149,9 @@ def test_other_workspace_sizes():
     for bad in (dict(B=0), dict(heads=0), dict(S=0), dict(budget=0)):
         with pytest.raises(q.QmvError):
             q.qmv_kv_evict_workspace_bytes(**{**dict(B=2, heads=4, S=100, budget=50), **bad})
+
+
+@pytest.mark.parametrize("wb,wh", [(0, 64), (256, 0), (256, 63), (255, 64), (63, 128), (64, 127), (0, 0), (-255, 64), (256, -63)])
+def test_attend_refuses_weights_that_overlap(wb, wh):
+    size = _attend_bytes(2, 4, 4, weights=1)[1]
+    assert attend(win=FAKE, wout=FAKE, S=64, wb=wb, wh=wh, ws=FAKE, wsb=size) == q.QMV_EINVAL and "overlap" in err()

@@ -312,3 +312,28 @@ def test_refusals(dev):
             (dict(q=torch.zeros(8 * 128 + 4, dtype=torch.bfloat16, device=dev)[4:].view(1, 8, 128)), "aligned")]:
         with pytest.raises(qm.QmvError, match=what):
             qm.qmv_kv_attend(**{**ok, **bad})
+
+
+def test_weights_in_other_layouts(dev):
+    """Heads before sequences, a head of its own, one sequence: any strides will
+    do as long as no two slots are one place; shared slots are refused."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    for B, heads in ((2, 2), (1, 3), (3, 1), (1, 1)):
+        lens = [40, 64, 9][:B]
+        tables, pages = ref.tables_for(lens, 16, B)
+        cache = ref.Cache(dev, pages, heads, 16, 128, seed=B)
+        q = ref.bf16_round(np.random.default_rng(1).standard_normal((B, heads * 2, 128)))
+        _, _, probs = ref.attend(q.double().numpy(), cache.k64, cache.v64, tables, lens, 16, 128 ** -0.5)
+        want = np.ones((B, heads, 80))
+        for b, p in enumerate(probs):
+            want[b, :, :p.shape[1]] += p.reshape(heads, 2, -1).sum(1)
+        call = dict(q=q.to(dev), k_cache=cache.k, v_cache=cache.v, block_tables=torch.from_numpy(tables).to(dev),
+                    lengths=torch.tensor(lens, dtype=torch.int32, device=dev))
+        for w in (torch.ones(heads, B, 80, device=dev).transpose(0, 1), torch.ones(B, heads + 1, 100, device=dev)[:, 1:, 20:]):
+            qm.qmv_kv_attend(weights=w, **call)
+            np.testing.assert_allclose(w.double().cpu().numpy(), want, rtol=0, atol=1e-4)
+        if B * heads > 1:
+            with pytest.raises(qm.QmvError, match="overlap"):
+                qm.qmv_kv_attend(weights=torch.ones(1, 1, 80, device=dev).expand(B, heads, 80), **call)
