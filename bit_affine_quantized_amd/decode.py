@@ -98,6 +98,13 @@ def _whole(spec, dtype, name, shape):
         step *= size
 
 
+def _slots(spec):
+    """(strides of axes 0 and 1, S) of a [B, heads, S] array; an axis of size one
+    has no stride."""
+    shape, stride = spec[0], spec[1]
+    return stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0, shape[2]
+
+
 def _workspace_ok(spec):
     if spec is not None:
         if spec[3].type != "cuda":
@@ -228,7 +235,7 @@ def _append_plan(k, v, kc, vc, tables, slots, rows, weights, positions, token_po
         _dev(t, dtype, name, 3)
         if tuple(t[0][:2]) != (B, heads):
             raise ValueError(f"{name} must be [{B}, {heads}, S], got {tuple(t[0])}")
-        mine = (t[1][0], t[1][1], t[0][2])
+        mine = _slots(t)
         if meta[2] and meta != mine:
             raise ValueError("weights and positions must have one shape and one layout")
         meta = mine
@@ -291,9 +298,9 @@ def _attend_plan(q, kc, vc, tables, lengths, mask, weights, weights_out, y, out_
             raise ValueError(f"weights must be [{B}, {heads}, S], got {tuple(shape)}")
         if weights_out is not None:
             _dev(weights_out, _F32, "weights_out", 3)
-            if weights_out[0] != shape or weights_out[1] != weights[1]:
+            if weights_out[0] != shape or _slots(weights_out) != _slots(weights):
                 raise ValueError("weights and weights_out must have one shape and one layout")
-        w = (weights[1][0], weights[1][1], shape[2])
+        w = _slots(weights)
     code, dtype = _out_code(out_dtype)
     if y is not None:
         _whole(y, dtype, "y", (B, Hq, D))
@@ -354,7 +361,7 @@ def _evict_plan(kc, vc, tables, lengths, weights, positions, nxt, out, workspace
     S = shape[2]
     if tuple(shape[:2]) != (B, heads) or positions[0] != shape or S == 0:
         raise ValueError(f"weights and positions must be [{B}, {heads}, S], got {tuple(shape)} and {tuple(positions[0])}")
-    if weights[1] != positions[1]:
+    if _slots(weights) != _slots(positions):
         raise ValueError("weights and positions must have one layout")
     _whole(lengths, _I32, "lengths", (B,))
     _whole(nxt, _I32, "next_positions", (B,))
@@ -365,7 +372,7 @@ def _evict_plan(kc, vc, tables, lengths, weights, positions, nxt, out, workspace
         _one_device(tables, *out)
     _workspace_ok(workspace)
     _one_device(tables, _first(kc), lengths, weights, positions, nxt, workspace)
-    return (dims, (tables[1][0] if B > 1 else cols, cols), B, (weights[1][0], weights[1][1], S),
+    return (dims, (tables[1][0] if B > 1 else cols, cols), B, _slots(weights),
             qmv_kv_evict_workspace_bytes(B, heads, S, budget))
 
 

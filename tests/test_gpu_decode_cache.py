@@ -358,3 +358,32 @@ def test_append_codes_of_groups_without_a_zero(dev, bits, gs):
         for t, want in zip(pool, (wq.view(np.int32), sc.view(np.int16), bi.view(np.int16))):
             got = _bits(t[at].transpose(1, 2).reshape(pages * page, heads, -1)[:T])
             np.testing.assert_array_equal(got.reshape(T * heads, -1), want)
+
+
+def test_bookkeeping_of_one_sequence_or_one_head(dev):
+    """An axis of size one may have any stride: weights and positions of one
+    sequence made in different ways have one layout."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    for B, heads in ((1, 2), (2, 1), (1, 1)):
+        S, n = 64, 48
+        cache = ref.Cache(dev, 4 * B, heads, 16, 128)
+        tables = torch.arange(4 * B, dtype=torch.int32, device=dev).view(B, 4)
+        lengths = torch.full((B,), n, dtype=torch.int32, device=dev)
+        w = torch.rand(B, heads, S, device=dev)
+        pos = torch.arange(S, dtype=torch.int32, device=dev).expand(B, heads, S).contiguous()
+        want = [t.clone() for t in qm.qmv_kv_evict(cache.k.clone(), cache.v.clone(), tables, lengths, w, pos, lengths, 20, recent=4)]
+        odd_w = torch.empty_strided((B, heads, S), (9999 if B == 1 else heads * S, 7777 if heads == 1 else S, 1), device=dev).copy_(w)
+        odd_p = pos
+        assert odd_w.stride() != odd_p.stride()
+        got = qm.qmv_kv_evict(cache.k.clone(), cache.v.clone(), tables, lengths, odd_w, odd_p, lengths, 20, recent=4)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        kv = ref.bf16_round(np.random.default_rng(0).standard_normal((B, 2 * heads, 128))).to(dev)
+        qm.qmv_kv_append(kv[:, :heads], kv[:, heads:], cache.k, cache.v, tables, lengths, weights=odd_w, positions=odd_p,
+                         token_positions=lengths + 100)
+        assert bool((odd_w[:, :, n] == 0).all()) and bool((odd_p[:, :, n] == n + 100).all())
+        q = ref.bf16_round(np.random.default_rng(1).standard_normal((B, heads, 128))).to(dev)
+        out = torch.empty(B, heads, S, device=dev)
+        qm.qmv_kv_attend(q, cache.k, cache.v, tables, lengths + 1, weights=odd_w, weights_out=out)
+        assert bool(((out - odd_w).sum(-1) - 1).abs().max() < 1e-3)
