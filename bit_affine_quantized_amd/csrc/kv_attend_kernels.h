@@ -152,10 +152,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   bf16x2 r = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
   return __builtin_bit_cast(uint32_t, r);
 }
-// c plus both bf16 values of a pair.
-__device__ __forceinline__ float add_pair(uint32_t pair, float c) {
+// c minus both bf16 values of a pair times the middle of what holds a code:
+// 127.5 (8 bits), 128 + 8 * 7.5 (4 bits).
+template <int BITS>
+__device__ __forceinline__ float take_mid(uint32_t pair, float c) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
+  constexpr uint32_t kMinusMid = BITS == 4 ? 0xC33CC33Cu : 0xC2FFC2FFu;
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, kMinusMid), c, false);
 }
 // The high halves of a and b, a's in the low half.
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
@@ -383,15 +386,17 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
   f32x4 o[OT];
   // A probability enters the values' product as the sum of its two terms T, off
   // by 2^-16 of itself, and a code as what holds it.  That error must not grow
-  // by how far the held codes are from zero, so
-  //   sum p v = sum T (held - kMid) + sum p v_mid,   v_mid the value at the middle code:
-  // the second sum in fp32, the terms' own sum beside it.
-  constexpr float kMid = BITS == 4 ? 188.0f : 127.5f;   // 128 + 8 * 7.5
-  float mid_sum[NG], term_sum[NG];
+  // by how far the held codes are from zero, so with their middle and the value
+  // v_mid there
+  //   sum p v = sum T held + sum (p v_mid - T middle),
+  // the second sum in fp32, in mid_sum.  Where columns 8..15 carry the second
+  // terms, the columns n and n + 8 are added in the end: each takes half of p v_mid.
+  constexpr float kHalf = HB == 8 ? 0.5f : 1.0f;
+  float mid_sum[NG];
 #pragma unroll
   for (int j = 0; j < OT; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int g = 0; g < NG; ++g) mid_sum[g] = term_sum[g] = 0.0f;
+  for (int g = 0; g < NG; ++g) mid_sum[g] = 0.0f;
   float m = -INFINITY, l = 0.0f;
   const float lazy = 8.0f * (a.natural == 1.0f ? 0.69314718055994531f : 1.0f);   // a factor of 2^8
   const float *mask = a.mask ? a.mask + b * a.mask_b + hq * a.mask_h : nullptr;
@@ -516,9 +521,9 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
         if constexpr (BITS == 4) {
           const float sk = across_halves(ak[g]);
           ak[g] = lane < 32 ? ak[g] * 0.125f : fmaf(-16.0f, sk, ak[g]);
-          av[g] = lane < 32 ? av[g] * 0.125f : fmaf(7.5f, sv, av[g]);
+          av[g] = lane < 32 ? av[g] * 0.125f : kHalf * fmaf(7.5f, sv, av[g]);
         } else {
-          av[g] = lane < 32 ? av[g] : fmaf(127.5f, sv, av[g]);
+          av[g] = lane < 32 ? av[g] : kHalf * fmaf(127.5f, sv, av[g]);
         }
         float *ka = reinterpret_cast<float *>(affine + (lane < 32 ? 0 : 1) * kArr);
         float *va = reinterpret_cast<float *>(affine + (lane < 32 ? 2 : 3) * kArr);
@@ -639,10 +644,7 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
 #pragma unroll
       for (int j = 0; j < OT; ++j) o[j] *= alpha;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        mid_sum[g] *= alpha;
-        term_sum[g] *= alpha;
-      }
+      for (int g = 0; g < NG; ++g) mid_sum[g] *= alpha;
     }
     const float base = m == -INFINITY ? 0.0f : m;
     float p[8];
@@ -694,8 +696,8 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
         ph[i] = pack_bf16(hi[2 * i], hi[2 * i + 1]);
         if constexpr (HB == 16) pl[i] = pack_bf16(lo[2 * i], lo[2 * i + 1]);
         if constexpr (CODES) {
-          term_sum[g] = add_pair(ph[i], term_sum[g]);
-          if constexpr (HB == 16) term_sum[g] = add_pair(pl[i], term_sum[g]);
+          mid_sum[g] = take_mid<BITS>(ph[i], mid_sum[g]);
+          if constexpr (HB == 16) mid_sum[g] = take_mid<BITS>(pl[i], mid_sum[g]);
         }
       }
       qmvk::static_for<0, VPL>([&](auto J) {
@@ -721,9 +723,7 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     mid_sum[g] = across_rows(mid_sum[g], add);
-    term_sum[g] = across_rows(term_sum[g], add);
-    if constexpr (HB == 8) term_sum[g] += __builtin_bit_cast(float, dpp<0x128>(__builtin_bit_cast(uint32_t, term_sum[g])));   // lane ^ 8
-    mid_sum[g] = fmaf(-kMid, term_sum[g], mid_sum[g]);
+    if constexpr (HB == 8) mid_sum[g] += __builtin_bit_cast(float, dpp<0x128>(__builtin_bit_cast(uint32_t, mid_sum[g])));   // lane ^ 8
   }
   if (kg == 0 && n < HB) {
     join_m(wave, n) = m;
