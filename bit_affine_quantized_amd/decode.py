@@ -195,11 +195,14 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _owner(stream):
     """Where a call's own allocations have to be made: memory of the current
     stream's pool may be in use there, and is handed out there again as soon as
     a workspace is dropped, whatever another stream is still doing with it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _ptr(t):
