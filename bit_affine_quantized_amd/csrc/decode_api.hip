@@ -84,9 +84,10 @@ struct AttendPlan {
 // if that makes 128 workgroups or more.  (bf16, 8 heads of 128, graph replays
 // on MI355X, chunks -> whole: one sequence of 128 / 512 / 640 / 1024 slots 10.1
 // -> 6.3, 10.1 -> 9.8, 10.2 -> 10.6, 10.3 -> 13.8 us, and 3 us less of launching
-// from the host; 16 sequences of 512 / 1024 / 2048: 12.3 -> 10.9, 20.1 -> 16.2,
-// 28.2 -> 25.9 us, but long batches of ragged lengths need the
-// sharing out that chunks give.)  Others are cut into chunks for workgroups of
+// from the host, so from 513 to 640 slots of few heads the one launch gains for a
+// caller that launches and loses 0.4 us in a graph; 16 sequences of 512 / 1024 /
+// 2048: 12.3 -> 10.9, 20.1 -> 16.2, 28.2 -> 25.9 us, but long batches of ragged
+// lengths need the sharing out that chunks give.)  Others are cut into chunks for workgroups of
 // four waves, about as many as the machine holds at once if that makes chunks
 // of kMostChunk slots at most, else so many of that size (1024 to 4096 measure
 // within 2% of each other).  The lengths are on the device, and so is the
@@ -263,7 +264,9 @@ struct BeamPlan {
   size_t m, l, left, list, bytes;
 };
 
-// Logits a thread of the scan: 32 where that leaves enough workgroups, else 16.
+// Logits a thread of the scan: 64 where that leaves 768 workgroups or more (16 x 8
+// beams over 131072: the scan 17.8 us with 32, 15.8 with 64), 32 where that
+// leaves 1024, else 16.
 BeamPlan beam_plan(int64_t rows, int64_t V, int num) {
   BeamPlan p{};
   p.per = rows * V >= int64_t(768) * kScanThreads * 64 ? 64 : (rows * V >= int64_t(1024) * kScanThreads * 32 ? 32 : 16);

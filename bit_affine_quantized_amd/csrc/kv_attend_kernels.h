@@ -20,12 +20,12 @@
 //
 // Why this shape, on MI355X: tiles in registers with one tile of loads in
 // flight behind the one at work, 2 (bf16 rows, D = 128) to 4 waves a SIMD.  32
-// sequences of 12000 to 16384 tokens, 8 heads of 128, 4 queries each, bf16: 319
-// to 327 us, 5.7 to 5.9 TB/s (without the tile ahead: 343); three waves a SIMD
+// sequences of 12000 to 16384 tokens, 8 heads of 128, 4 queries each, bf16: 320
+// to 329 us, 5.7 to 5.8 TB/s (without the tile ahead: 343); three waves a SIMD
 // spill (336 -> 343 in a graph).  131071 tokens, 8-bit rows, 8 queries each: 68
 // us (4.2 TB/s; without the tile ahead 118); 40 us of it are its loop, 5 to 16
 // the wait for lengths, then pages, then rows, while other workgroups' loads
-// already queue.  24 sequences of 16 heads of 64, 4-bit rows: 24 us, bound by
+// already queue.  24 sequences of 16 heads of 64, 4-bit rows: 25 us, bound by
 // vector instructions (about 300 a tile of 2.5 KB: unpacking, softmax, splits).
 
 #pragma once
@@ -72,8 +72,9 @@ constexpr int kChunkWaves = 4;                 // waves a workgroup that takes a
 static_assert(kChunkUnit == kChunkWaves * kTile, "a tile for every wave");
 
 // Waves a SIMD that an instance's registers are shared out for: as many as fit
-// without spilling in the loop (bf16 rows are held in registers, codes go
-// through LDS).
+// with hardly a spill (bf16 rows are held in registers, codes go through LDS;
+// bf16 and 4-bit rows spill none, 8-bit rows up to 9 registers at D = 128 and, in
+// groups of 32, 83 at D = 256).
 constexpr int attend_waves(int D, int bits) {
   return D == 64 ? 4 : D == 128 ? (bits == 16 ? 2 : 3) : (bits == 16 ? 1 : 2);
 }
@@ -655,8 +656,10 @@ __global__ __launch_bounds__(64 * attend_most_waves(S::D), attend_waves(S::D, S:
     }
 
     // Values: out^T += V^T P^T, the probabilities as two bf16 terms (high and
-    // low), which keeps 16 bits of them.  With at most 8 heads the columns
-    // 8..15 carry the low terms, so one product does both.
+    // low), which keeps 16 bits of them: outputs are off by 3e-6 to 4e-6 of their
+    // size (root mean square, all row types), a few thousandths of a bf16 output's
+    // rounding.  A third term would take a product more a tile.  With at most 8
+    // heads the columns 8..15 carry the low terms, so one product does both.
     if constexpr (CODES) {
       stage_codes(value_codes);
       if constexpr (!kLast) load_values(ahead);

@@ -18,7 +18,9 @@ template <typename S>
 int launch_attend(const AttendArgs &a, int64_t chunks, hipStream_t st) {
   const int64_t blocks = chunks * a.heads * a.head_blocks;
   if (blocks > 0x7FFFFFFF) return fail(QMV_EUNSUPPORTED, "qmv_kv_attend: too many workgroups");
-  const int lds = 4 * a.waves * attend_wave_lds(S::D, S::BITS, S::NG, S::HB);   // at most 126 KiB
+  constexpr int kWave = 4 * attend_wave_lds(S::D, S::BITS, S::NG, S::HB);
+  static_assert(attend_most_waves(S::D) * kWave <= 67 * 1024, "two workgroups of the most waves a CU");
+  const int lds = a.waves * kWave;
   auto kern = attend_kernel<S>;
   if (lds > 64 * 1024)
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,

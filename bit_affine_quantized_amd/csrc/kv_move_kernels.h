@@ -14,7 +14,7 @@ namespace qmvd {
 // rows[t] (t itself without `rows`).  A negative slot, a sequence or a page
 // that does not exist writes nothing.  A decode step's append (64 tokens, 8
 // heads of 128, bf16) takes 3.1 us, a launch and one chain of three loads.
-// Four prompts of 2047 tokens into 8-bit rows, 51 MB in all: 22 us (2.4 TB/s),
+// Four prompts of 2047 tokens into 8-bit rows, 51 MB in all: 21 us (2.4 TB/s),
 // bound by the vector instructions of the rounding and by two rounds of that
 // chain; with 64-bit divisions in the indexing and true ones in the rounding
 // it took 27.
