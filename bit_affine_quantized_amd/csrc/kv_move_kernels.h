@@ -75,12 +75,13 @@ struct Quantized {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(raw[e] << 16);
-      x[2 * e + 1] = __uint_as_float(raw[e] & 0xFFFF0000u);
+      // a signalling NaN would not be passed over by min and max, but end them
+      x[2 * e] = __builtin_canonicalizef(__uint_as_float(raw[e] << 16));
+      x[2 * e + 1] = __builtin_canonicalizef(__uint_as_float(raw[e] & 0xFFFF0000u));
     }
     float lo = FLT_MAX, hi = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {           // fminf would first quiet each operand
+    for (int e = 0; e < 8; e += 2) {           // fminf would quiet each operand once more
       asm("v_min3_f32 %0, %0, %1, %2" : "+v"(lo) : "v"(x[e]), "v"(x[e + 1]));
       asm("v_max3_f32 %0, %0, %1, %2" : "+v"(hi) : "v"(x[e]), "v"(x[e + 1]));
     }
@@ -117,7 +118,8 @@ struct Quantized {
     for (int e = 0; e < 8; ++e) {
       const float r = quick_quotient(x[e], z, inverse);
       far = fmaxf(far, fabsf(r - __builtin_rintf(r)));
-      byte[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(BITS == 8 ? r : fminf(r, top), e % 4, byte[e / 4]);   // 0 to 255
+      // 0 to 255, NaN as 0; the median of NaN and two numbers is the smaller one
+      byte[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(BITS == 8 ? r : __builtin_amdgcn_fmed3f(r, 0.0f, top), e % 4, byte[e / 4]);
     }
     if (!(far < 0.5f - kNear)) {
       byte[0] = byte[1] = 0u;
