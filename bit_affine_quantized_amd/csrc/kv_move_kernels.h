@@ -511,8 +511,9 @@ __device__ __forceinline__ void evict_meta(const EvictArgs &a, int bh, int b, in
   const int keep = n < a.budget ? n : a.budget;
   const int64_t in = b * a.meta_b + h * a.meta_h, out = static_cast<int64_t>(bh) * a.S;
   const uint64_t *stay = a.stay + static_cast<int64_t>(bh) * a.mask_words;
-  for (int i = part * kMoveThreads + threadIdx.x; i < a.S; i += parts * kMoveThreads) {
-    if (i >= keep) {
+  // unsigned: the step past the last slot can pass 2^31
+  for (uint32_t i = part * kMoveThreads + threadIdx.x; i < static_cast<uint32_t>(a.S); i += parts * kMoveThreads) {
+    if (i >= static_cast<uint32_t>(keep)) {
       a.weights_out[out + i] = 0.0f;
       a.positions_out[out + i] = -1;
     } else if (count == 0 || ((stay[(i >> 8) * 4 + (i & 3)] >> ((i >> 2) & 63)) & 1)) {

@@ -387,3 +387,26 @@ def test_bookkeeping_of_one_sequence_or_one_head(dev):
         out = torch.empty(B, heads, S, device=dev)
         qm.qmv_kv_attend(q, cache.k, cache.v, tables, lengths + 1, weights=odd_w, weights_out=out)
         assert bool(((out - odd_w).sum(-1) - 1).abs().max() < 1e-3)
+
+
+def test_evict_bookkeeping_of_the_most_slots(dev):
+    """Bookkeeping as wide as is accepted (8.6 GB an array): what lies past the
+    new length is cleared up to the last slot."""
+    import torch
+
+    import bit_affine_quantized_amd as qm
+    S, n = 2 ** 31 - 1 - 65536, 100
+    cache = ref.Cache(dev, 8, 1, 16, 128)
+    tables = torch.arange(8, dtype=torch.int32, device=dev)[None]
+    lengths = torch.tensor([n], dtype=torch.int32, device=dev)
+    w = torch.ones(1, 1, S, device=dev)
+    pos = torch.ones(1, 1, S, dtype=torch.int32, device=dev)
+    got = qm.qmv_kv_evict(cache.k, cache.v, tables, lengths, w, pos, lengths, 60)
+    assert int(got[0]) == 60
+    assert bool((got[1][..., :60] == 1).all()) and bool((got[2][..., :60] == 1).all())
+    for t, want in ((got[1], 0), (got[2], -1)):
+        for a in range(0, S, 1 << 28):
+            part = t[0, 0, max(a, 60):min(S, a + (1 << 28))]
+            assert int(part.min()) == want and int(part.max()) == want
+    del w, pos, got, t, part
+    torch.cuda.empty_cache()
