@@ -63,7 +63,7 @@ int check_tables(const char *fn, const qmv_kv_cache *c, const int32_t *tables, i
   if (B < 1 || cols < 1) return fail(QMV_EINVAL, "%s: B=%lld and cols=%lld must be positive", fn, (long long)B, (long long)cols);
   if (B > (1 << 24)) return fail(QMV_EINVAL, "%s: B=%lld too large", fn, (long long)B);
   if (ld < cols) return fail(QMV_EINVAL, "%s: table stride %lld below cols=%lld", fn, (long long)ld, (long long)cols);
-  if (cols * c->page_size > kMaxSlots) return fail(QMV_EINVAL, "%s: cols * page_size too large", fn);
+  if (cols > kMaxSlots / c->page_size) return fail(QMV_EINVAL, "%s: cols * page_size too large", fn);
   return QMV_OK;
 }
 
@@ -131,7 +131,7 @@ AttendPlan attend_plan(const qmv_kv_cache &c, int64_t B, int64_t cols, int group
 int check_attend(const char *fn, const qmv_kv_cache *c, int64_t B, int64_t cols, int group, int64_t max_length) {
   if (int rc = check_cache(fn, c)) return rc;
   if (B < 1 || B > (1 << 24)) return fail(QMV_EINVAL, "%s: B=%lld out of range", fn, (long long)B);
-  if (cols < 1 || cols * c->page_size > kMaxSlots) return fail(QMV_EINVAL, "%s: cols=%lld out of range", fn, (long long)cols);
+  if (cols < 1 || cols > kMaxSlots / c->page_size) return fail(QMV_EINVAL, "%s: cols=%lld out of range", fn, (long long)cols);
   const int64_t cap = cols * c->page_size, longest = max_length > 0 && max_length < cap ? max_length : cap;
   if (B * longest > int64_t(1) << 35)
     return fail(QMV_EUNSUPPORTED, "%s: %lld sequences of up to %lld slots are too many", fn, (long long)B, (long long)longest);
@@ -254,7 +254,8 @@ int check_evict(const char *fn, int64_t B, int heads, int64_t S, int64_t budget)
   if (B < 1 || B > (1 << 24) || heads < 1) return fail(QMV_EINVAL, "%s: B=%lld or heads=%d out of range", fn, (long long)B, heads);
   if (S < 1 || S > kMaxSlots) return fail(QMV_EINVAL, "%s: S=%lld out of range", fn, (long long)S);
   if (budget < 1 || budget > kMaxSlots) return fail(QMV_EINVAL, "%s: budget=%lld must be positive", fn, (long long)budget);
-  if (B * heads > 0x7FFFFFFF) return fail(QMV_EUNSUPPORTED, "%s: too many heads", fn);
+  if (B * heads > 0x7FFFFFFF || B * heads > (int64_t(1) << 40) / S)
+    return fail(QMV_EUNSUPPORTED, "%s: %lld sequences of %d heads with S=%lld are too many", fn, (long long)B, heads, (long long)S);
   return QMV_OK;
 }
 
@@ -513,6 +514,8 @@ int qmv_beam_reorder(const qmv_kv_cache *cache, const int32_t *block_tables, con
   if (!lengths || !parents || !spare_pages || !tables_out || !lengths_out) return fail(QMV_EINVAL, "%s: null array", fn);
   if (parents_ld < M) return fail(QMV_EINVAL, "%s: parents stride %lld below M=%lld", fn, (long long)parents_ld, (long long)M);
   if (tables_out == block_tables || lengths_out == lengths) return fail(QMV_EINVAL, "%s: the outputs must not be the inputs", fn);
+  if (static_cast<int64_t>(cache->heads) * cache->page_size > kMaxSlots)   // a page's rows are numbered in 32 bits
+    return fail(QMV_EUNSUPPORTED, "%s: %d heads of %d slots a page are too many", fn, cache->heads, cache->page_size);
   ReorderArgs a{};
   a.pool = pools_of(*cache);
   a.tables = block_tables;

@@ -259,7 +259,9 @@ int qmv_unpack_codes(const uint32_t *w_q, int64_t N, int64_t K, int bits,
  * kernels on `stream` have finished, and need no clearing.
  * Scales and biases are aligned to a row's 2 * (head_dim / group_size) bytes.
  * Also QMV_EUNSUPPORTED: an append of more than 2^30 - 1 tokens times heads;
- * attention over more than 2^35 slots, sequences times the longest.
+ * attention over more than 2^35 slots, sequences times the longest; eviction from
+ * more than 2^40 entries, sequences times heads times S; reordering of pages of
+ * 2^31 rows, heads times slots.
  * ---------------------------------------------------------------------------
  */
 typedef struct qmv_kv_cache {

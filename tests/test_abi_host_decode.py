@@ -155,3 +155,16 @@ def test_other_workspace_sizes():
 def test_attend_refuses_weights_that_overlap(wb, wh):
     size = _attend_bytes(2, 4, 4, weights=1)[1]
     assert attend(win=FAKE, wout=FAKE, S=64, wb=wb, wh=wh, ws=FAKE, wsb=size) == q.QMV_EINVAL and "overlap" in err()
+
+
+def test_sizes_that_pass_64_or_32_bits_are_refused():
+    out = ctypes.c_size_t(7)
+    for B, heads, S, budget in ((1 << 24, 127, (1 << 31) - 65537, 1 << 30), (1 << 24, 64, 1 << 30, 1 << 29), (1 << 10, 1 << 10, (1 << 20) + 1, 5)):
+        assert q.lib().qmv_kv_evict_workspace_bytes(B, heads, S, budget, ctypes.byref(out)) == q.QMV_EUNSUPPORTED and "too many" in err()
+    assert q.lib().qmv_kv_evict_workspace_bytes(1 << 10, 1 << 10, 1 << 20, 5, ctypes.byref(out)) == q.QMV_OK and out.value > 0
+    big = dict(page=1 << 20, cols=1 << 50, ld=1 << 50)
+    for call in (append, attend):
+        c = cache(page=big["page"])
+        assert call(c, cols=big["cols"], ld=big["ld"]) == q.QMV_EINVAL and ("too large" in err() or "out of range" in err())
+    assert _attend_bytes(1, 1 << 50, 4, page=1 << 20)[0] == q.QMV_EINVAL
+    assert reorder(cache(heads=1 << 12, page=1 << 20)) == q.QMV_EUNSUPPORTED and "too many" in err()
