@@ -1,9 +1,8 @@
-// The appended codes' short cut (csrc/append_quick.h) against the divisions,
-// over groups of bf16 values all above zero, of narrow and wide range, and over
-// groups with values on both sides: every (largest, smallest, value) of a few
-// of the first kind with the largest in [1, 2) and the smallest from 1/2 on, a grid of
-// the others; with the reciprocal exact and one unit off either way.  Prints the
-// number of values compared, then "ok".
+// The appended codes' short cut (csrc/append_quick.h) against the divisions:
+// every (largest, smallest, value) of the groups of bf16 values above zero with
+// the largest in [1, 2) and the smallest from 1/2 on, and a grid of groups with
+// values far apart or on both sides; with the reciprocal exact and one unit off
+// either way.  Prints the number of values compared, then "ok".
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
